@@ -599,6 +599,8 @@ ck4_status ck4_qk_norm_rope_backward(const uint16_t *dq_out, int64_t dqo_st, int
  *     ascending from 0 to tq and tk; empty sequences are allowed. Both NULL:
  *     one sequence of all rows (seqs = 1). The contents are not checked; values outside
  *     [0, tq], [0, tk] are clamped, and rows that no sequence has are not written.
+ *     Starts out of order leave open which rows are written; nothing but the outputs
+ *     and the workspace is.
  *   causal  row i of a sequence with nq queries and nk keys sees the keys
  *     j <= i + nk - nq; else all nk.
  *   scale   positive, at most 1e6 (larger ones are unsupported).

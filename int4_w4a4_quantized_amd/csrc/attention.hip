@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_join_kernel(Attn a, HeadsOu
     const int head = blockIdx.x / deal.tiles;
     Span s;
     if (!find_tile<kRows, false>(a.rows, blockIdx.x % deal.tiles, &s)) return;
-    const Parts parts = Parts::of<kRows, false>(a.rows, a.causal, a.hq, 1, s, head);
+    const Parts parts = Parts::of<kRows, false>(a.rows, a.causal, a.hq, 1, deal.most, s, head);
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, h = lane / 32;
     const int row = s.tile * kRows + wave * 32 + lane % 32;
     if (!parts.cut() || row >= s.nq) return;
@@ -283,9 +283,9 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_join_kernel(Attn a, HeadsOu
 }
 
 template <int D>
-hipError_t launch_fwd(const Attn &a, const HeadsOut &out, float *lse, float *partial, hipStream_t stream) {
+hipError_t launch_fwd(const Attn &a, const HeadsOut &out, float *lse, int most, float *partial, hipStream_t stream) {
     const int64_t tiles = most_tiles(a.rows.tq, kRows, a.rows.seqs, a.rows.cu_q != nullptr);
-    const Deal deal{(int)tiles, partial};
+    const Deal deal{(int)tiles, most, partial};
     attn_fwd_kernel<D><<<dim3(grid_of(deal, a.hq)), kThreads, 0, stream>>>(FwdArgs{a, out, lse, deal});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !partial) return e;
@@ -296,14 +296,14 @@ hipError_t launch_fwd(const Attn &a, const HeadsOut &out, float *lse, float *par
 }  // namespace
 
 int64_t attention_floats(int seqs, int64_t tq, int64_t tk, int hq, int d) {
-    return partial_floats(most_tiles(tq, kRows, seqs, true) * hq, (tk + kTile - 1) / kTile,
-                          d <= 64 ? kPartial<64> : kPartial<128>);
+    return partial_floats(most_steps<kRows, false>(seqs, tq, tk, hq, 1), d <= 64 ? kPartial<64> : kPartial<128>);
 }
 
 hipError_t launch_attention(const Attn &a, const HeadsOut &out, float *lse, float *workspace, hipStream_t stream) {
-    float *partial = attention_floats(a.rows.seqs, a.rows.tq, a.rows.tk, a.hq, a.d) ? workspace : nullptr;
-    if (a.d <= 64) return launch_fwd<64>(a, out, lse, partial, stream);
-    return launch_fwd<128>(a, out, lse, partial, stream);
+    const int most = most_steps<kRows, false>(a.rows.seqs, a.rows.tq, a.rows.tk, a.hq, 1);
+    float *partial = most ? workspace : nullptr;
+    if (a.d <= 64) return launch_fwd<64>(a, out, lse, most, partial, stream);
+    return launch_fwd<128>(a, out, lse, most, partial, stream);
 }
 
 }  // namespace ck4

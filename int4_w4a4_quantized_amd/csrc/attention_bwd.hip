@@ -439,7 +439,7 @@ __device__ __forceinline__ void join_grads(const Attn &a, const HeadsOut &o0, co
     Span s;
     if (!find_tile<kRows, KEYS>(a.rows, item % deal.tiles, &s)) return;
     const Parts parts =
-        Parts::of<kRows, KEYS>(a.rows, a.causal, KEYS ? a.hk : a.hq, KEYS ? a.hq / a.hk : 1, s, head);
+        Parts::of<kRows, KEYS>(a.rows, a.causal, KEYS ? a.hk : a.hq, KEYS ? a.hq / a.hk : 1, deal.most, s, head);
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, h = lane / 32;
     const int row = s.tile * kRows + wave * 32 + lane % 32;
     if (!parts.cut() || row >= (KEYS ? s.nk : s.nq)) return;
@@ -475,12 +475,17 @@ __global__ __launch_bounds__(kThreads) void attn_grad_join_kernel(BwdArgs k) {
         join_grads<D, false>(k.a, k.dq, k.dq, k.queries, item - keys);
 }
 
+// Steps of the line of all tiles of queries, and of keys.
+int most_q(int seqs, int64_t tq, int64_t tk, int hq) { return most_steps<kRows, false>(seqs, tq, tk, hq, 1); }
+int most_kv(int seqs, int64_t tq, int64_t tk, int hq, int hk) { return most_steps<kRows, true>(seqs, tq, tk, hk, hq / hk); }
+
 template <int D>
 hipError_t launch_bwd(const Attn &a, const Heads &dout, const float *stat, float *part_q, float *part_kv, const HeadsOut &dq,
                       const HeadsOut &dk, const HeadsOut &dv, hipStream_t stream) {
-    const bool packed = a.rows.cu_q != nullptr;
-    const Deal qd{(int)most_tiles(a.rows.tq, kRows, a.rows.seqs, packed), part_q};
-    const Deal kd{(int)most_tiles(a.rows.tk, kRows, a.rows.seqs, packed), part_kv};
+    const Packed &r = a.rows;
+    const bool packed = r.cu_q != nullptr;
+    const Deal qd{(int)most_tiles(r.tq, kRows, r.seqs, packed), most_q(r.seqs, r.tq, r.tk, a.hq), part_q};
+    const Deal kd{(int)most_tiles(r.tk, kRows, r.seqs, packed), most_kv(r.seqs, r.tq, r.tk, a.hq, a.hk), part_kv};
     const unsigned keys = grid_of(kd, a.hk), queries = grid_of(qd, a.hq);
     BwdArgs args{a, dout, stat, dq, dk, dv, kd, qd, keys};
     if (part_q || part_kv || keys + queries <= kPieces) {
@@ -498,12 +503,10 @@ hipError_t launch_bwd(const Attn &a, const Heads &dout, const float *stat, float
 }
 
 int64_t floats_q(int seqs, int64_t tq, int64_t tk, int hq, int d) {
-    return partial_floats(most_tiles(tq, kRows, seqs, true) * hq, (tk + kTile - 1) / kTile,
-                          d <= 64 ? kPartialQ<64> : kPartialQ<128>);
+    return partial_floats(most_q(seqs, tq, tk, hq), d <= 64 ? kPartialQ<64> : kPartialQ<128>);
 }
 int64_t floats_kv(int seqs, int64_t tq, int64_t tk, int hq, int hk, int d) {
-    return partial_floats(most_tiles(tk, kRows, seqs, true) * hk, (tq + kTile - 1) / kTile * (hq / hk),
-                          d <= 64 ? kPartialKV<64> : kPartialKV<128>);
+    return partial_floats(most_kv(seqs, tq, tk, hq, hk), d <= 64 ? kPartialKV<64> : kPartialKV<128>);
 }
 int64_t floats_stat(int64_t tq, int hq) { return (2 * tq * hq + 3) / 4 * 4; }
 

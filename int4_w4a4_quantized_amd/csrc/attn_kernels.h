@@ -56,8 +56,9 @@ hipError_t launch_qk_norm_rope_backward(const NormRope &a, const Heads dy[2], co
 
 // Packed sequences: sequence i owns rows [cu[i], cu[i + 1]) of its tensor,
 // cu int32 [seqs + 1] on the device (null: one sequence of all rows). The
-// kernels clamp what they read from cu to [0, rows], so no content makes them
-// leave the tensors.
+// kernels clamp what they read from cu to [0, rows], and cut tiles only where
+// the steps that they count fit what the workspace was sized for, so no content
+// makes them leave the tensors or the workspace.
 struct Packed {
     const int32_t *cu_q, *cu_k;
     int64_t tq, tk;

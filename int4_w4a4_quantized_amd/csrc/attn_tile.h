@@ -26,7 +26,7 @@
 #include <limits.h>
 #include <stdint.h>
 
-#include "attn_kernels.h"
+#include "attn_line.h"
 
 namespace ck4 {
 namespace {
@@ -40,7 +40,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 64;             // rows of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -265,35 +264,17 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
     return v;
 }
 
-// One sequence's rows, and the tile of them that a workgroup has.
-struct Span {
-    int q0, k0;
-    int nq, nk;
-    int tile, tiles;
-    int seq;
-};
-
-__device__ __forceinline__ int clamp_row(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
-
 __device__ __forceinline__ Span span_of(const Packed &p, int i) {
     Span s{};
-    s.seq = i;
-    s.nq = (int)p.tq;
-    s.nk = (int)p.tk;
     if (p.cu_q) {
         const auto cu_q = global(p.cu_q), cu_k = global(p.cu_k);
-        s.q0 = clamp_row(cu_q[i], 0, s.nq);
-        s.k0 = clamp_row(cu_k[i], 0, s.nk);
-        s.nq = clamp_row(cu_q[i + 1], s.q0, s.nq) - s.q0;
-        s.nk = clamp_row(cu_k[i + 1], s.k0, s.nk) - s.k0;
+        s = span_between((int)p.tq, (int)p.tk, cu_q[i], cu_q[i + 1], cu_k[i], cu_k[i + 1]);
+    } else {
+        s.nq = (int)p.tq;
+        s.nk = (int)p.tk;
     }
+    s.seq = i;
     return s;
-}
-
-// Row `row` of a sequence sees the first limit() keys.
-__device__ __forceinline__ int limit(const Span &s, bool causal, int row) {
-    const int n = causal ? row - s.nq + s.nk + 1 : s.nk;
-    return n < 0 ? 0 : n > s.nk ? s.nk : n;
 }
 
 // The same values in every lane, kept in scalar registers.
@@ -326,116 +307,39 @@ __device__ __forceinline__ bool find_tile(const Packed &p, int tile, Span *out) 
     return false;
 }
 
-// Upper bound of the tiles over all sequences.
-inline int64_t most_tiles(int64_t rows_total, int rows, int seqs, bool packed) {
-    return (rows_total + rows - 1) / rows + (packed ? seqs : 0);
-}
-
 // Workgroups are dealt to the 8 XCDs in turn. Work item of a workgroup such
 // that each XCD has a contiguous range of the items (whole heads, mostly),
 // whose keys and values then stay in its own L2. grid: a multiple of 8.
 __device__ __forceinline__ int xcd_item(unsigned group, unsigned grid) { return (int)(group % 8 * (grid / 8) + group / 8); }
 
-// Where there are too few tiles for the card's compute units, the steps of all
-// tiles (64 keys each, or 64 queries of one head) form one line, which is cut
-// into equal pieces, one per workgroup. A tile that no piece has whole is
-// left as partial results and joined by a second kernel, in the order of the
-// pieces. If no tile is much longer than a piece would be, whole tiles are
-// dealt all the same.
-//
-// Steps of the tiles t of one sequence and head: c, or, in a causal sequence,
-// clamp(a + B t, 1, c). A tile without any work counts as one step, so that its
-// rows are written.
-template <int B>
-struct Ramp {
-    int a, c;
-    int tiles, mul;  // mul: the query heads of a key head, where they are walked one by one
-    bool rising;
-
-    __device__ __forceinline__ int steps(int t) const { return (rising ? clamp_row(a + B * t, 1, c) : c) * mul; }
-    // steps of the tiles before t
-    __device__ __forceinline__ int before(int t) const {
-        // the first tiles with more than one step and with c, t at most
-        const int n0 = rising ? clamp_row((B - a) / B, 0, t) : 0;
-        const int n1 = rising ? clamp_row((c - a + B - 1) / B, n0, t) : 0;
-        return (n0 + a * (n1 - n0) + B * ((n1 * (n1 - 1) - n0 * (n0 - 1)) / 2) + c * (t - n1)) * mul;
-    }
-};
-
-// KEYS: tiles of ROWS keys, in falling order, stepping over queries; else
-// tiles of ROWS queries stepping over keys.
+// The line of all steps, cut into pieces.
 template <int ROWS, bool KEYS>
-__device__ __forceinline__ Ramp<ROWS / kTile> ramp_of(const Span &s, bool causal, int group) {
-    static_assert(ROWS % kTile == 0, "whole steps");
-    const int shift = s.nk - s.nq, walked = ((KEYS ? s.nq : s.nk) + kTile - 1) / kTile;
-    Ramp<ROWS / kTile> r;
-    r.tiles = ((KEYS ? s.nk : s.nq) + ROWS - 1) / ROWS;
-    r.c = walked > 1 ? walked : 1;
-    r.a = KEYS ? walked - (((r.tiles - 1) * ROWS - shift) >> 6) : (ROWS + shift + kTile - 1) >> 6;
-    r.mul = KEYS ? group : 1;
-    r.rising = causal;
-    return r;
-}
-
-constexpr int kPieces = 256;  // one workgroup a compute unit: its 8 wavefronts of up to 256 registers fill it
-constexpr int kLeast = 4;     // steps of a piece at least
-// Tiles are cut where the longest takes at least so many steps more than a piece: the partial results and their
-// joining take about as long.
-constexpr int kGain = 16;
-
-// The line of all steps: `count` pieces (0: whole tiles are dealt) of size or size + 1 steps, the first `more` of them.
-template <int ROWS, bool KEYS>
-struct Pieces {
+struct Pieces : Cut {
     const Packed &p;
     bool causal;
     int heads, group;
-    int total, count, size, more;
 
-    __device__ __forceinline__ Ramp<ROWS / kTile> ramp(int i) const { return ramp_of<ROWS, KEYS>(span_of(p, i), causal, group); }
+    static __device__ __forceinline__ Ramp<ROWS / kTile> ramp(const Packed &p, bool causal, int group, int i) {
+        return ramp_of<ROWS, KEYS>(span_of(p, i), causal, group);
+    }
     __device__ __forceinline__ int all_steps(int i) const {
-        const auto r = ramp(i);
+        const auto r = ramp(p, causal, group, i);
         return r.before(r.tiles) * heads;
     }
-    __device__ __forceinline__ Pieces(const Packed &p_, bool causal_, int heads_, int group_)
-        : p(p_), causal(causal_), heads(heads_), group(group_) {
+    static __device__ __forceinline__ LineSum sum(const Packed &p, bool causal, int heads, int group, int most) {
         const int lane = thread_again() % 64;
-        int n = 0, longest = 0;
+        LineSum s;
 #pragma unroll 1
-        for (int i = lane; i < p.seqs; i += 64) {
-            const auto r = ramp(i);
-            n += r.before(r.tiles) * heads;
-            longest = max(longest, r.tiles ? r.steps(r.tiles - 1) : 0);
-        }
-        total = wave_sum(n, lane);
-        longest = wave_max(longest, lane);
-        count = min((total + kLeast - 1) / kLeast, kPieces);
-        size = total / max(count, 1);
-        more = total - size * count;
-        if (longest < size + kGain) count = 0;
+        for (int i = lane; i < p.seqs; i += 64) s.add(ramp(p, causal, group, i), heads, most);
+#pragma unroll 1
+        for (int step = 32; step > 0; step /= 2) s.total = add_steps(s.total, from_lane(s.total, lane ^ step), most);
+        s.total = __builtin_amdgcn_readfirstlane(s.total);
+        s.longest = wave_max(s.longest, lane);
+        return s;
     }
-    __device__ __forceinline__ int start(int piece) const { return piece * size + min(piece, more); }
-    __device__ __forceinline__ int piece_of(int at) const {
-        const int big = more * (size + 1);
-        return at < big ? at / (size + 1) : more + (at - big) / size;
-    }
+    __device__ __forceinline__ Pieces(const Packed &p_, bool causal_, int heads_, int group_, int most)
+        : Cut(sum(p_, causal_, heads_, group_, most), most), p(p_), causal(causal_), heads(heads_), group(group_) {}
 };
-
-// How a launch deals its tiles: each to a workgroup of its own (partial null),
-// or by Pieces, whose partial results go to `partial`: piece w leaves at most two,
-// of the tile that it begins in at place 2 w and of the one that it ends in at 2 w + 1.
-struct Deal {
-    int tiles;  // upper bound, per head
-    float *partial;
-};
-
-// Floats of workspace of a launch with `tiles` tiles (upper bound, over all heads) of `steps` steps at most, of `each`
-// floats a partial result; 0: whole tiles are dealt. From kFewTiles tiles on the compute units have work enough.
-constexpr int64_t kFewTiles = 256;
-inline int64_t partial_floats(int64_t tiles, int64_t steps, int64_t each) {
-    if (tiles >= kFewTiles || steps <= kGain || tiles * steps > INT_MAX / 2) return 0;
-    const int64_t fit = (tiles * steps + kLeast - 1) / kLeast;
-    return 2 * (fit < kPieces ? fit : kPieces) * each;
-}
 
 // A kernel's arguments (one struct), read again from where they are. Kernels that walk over several parts of tiles read
 // them for each: kept across a part's steps, they would push the steps' own values out of the scalar registers.
@@ -459,11 +363,6 @@ struct Segment {
     int from, to;
 };
 
-// The workgroups of a launch: one a tile (over all heads), or one a piece.
-inline unsigned grid_of(const Deal &d, int heads) {
-    return (unsigned)(d.partial ? kPieces : ((int64_t)d.tiles * heads + 7) / 8 * 8);
-}
-
 // A workgroup's way through its piece of the line: what is left of it, and the tile that it is in.
 struct Cursor {
     int left = 0;
@@ -485,7 +384,7 @@ __device__ __forceinline__ bool next_segment(unsigned group_id, unsigned groups,
     g->to = INT_MAX;
     *partial = nullptr;
     if (!whole && c.begins) {
-        const Pieces<ROWS, KEYS> pieces(p, causal, heads, group);
+        const Pieces<ROWS, KEYS> pieces(p, causal, heads, group, d.most);
         whole = pieces.count == 0;
         if (!whole) {
             if (item >= pieces.count) return false;
@@ -549,7 +448,7 @@ __device__ __forceinline__ bool next_segment(unsigned group_id, unsigned groups,
     g->s.tile = KEYS ? r.tiles - 1 - c.t : c.t;
     g->s.tiles = r.tiles;
     g->to = min(g->from + c.left, steps);
-    if (g->from > 0 || g->to < steps) *partial = d.partial + (2 * item + (c.begins ? 0 : 1)) * each;
+    if (g->from > 0 || g->to < steps) *partial = d.partial + Cut::place(item, c.begins) * each;
     c.left -= g->to - g->from;
     c.begins = false;
     c.done = c.left <= 0;
@@ -562,9 +461,10 @@ struct Parts {
     bool begins;      // the first piece begins with the tile
 
     template <int ROWS, bool KEYS>
-    static __device__ __forceinline__ Parts of(const Packed &p, bool causal, int heads, int group, const Span &s, int head) {
+    static __device__ __forceinline__ Parts of(const Packed &p, bool causal, int heads, int group, int most, const Span &s,
+                                               int head) {
         Parts r{0, 0, false};
-        const Pieces<ROWS, KEYS> pieces(p, causal, heads, group);
+        const Pieces<ROWS, KEYS> pieces(p, causal, heads, group, most);
         if (pieces.count == 0) return r;
         const int lane = thread_again() % 64;
         int n = 0;
@@ -580,7 +480,7 @@ struct Parts {
     }
     __device__ __forceinline__ bool cut() const { return last > first; }
     __device__ __forceinline__ const float *at(const float *partial, int w, int64_t each) const {
-        return partial + (2 * w + (w == first && !begins ? 1 : 0)) * each;
+        return partial + Cut::place(w, w != first || begins) * each;
     }
 };
 constexpr int kJoinBlocks = 8;  // workgroups a tile that share its partial results' values

@@ -327,6 +327,31 @@ def test_attention_starts_out_of_range(ck):
         assert torch.isfinite(b.float()).all() and (b[:100] == 3).all() and (b[200:] == 3).all()
 
 
+@pytest.mark.parametrize("tq,tk,seqs,hq,hk,d", [
+    (1024, 1344, 3, 1, 1, 128), (2560, 1280, 10, 1, 1, 64), (2560, 1280, 9, 2, 1, 128), (700, 4000, 30, 4, 2, 72),
+])
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_starts_out_of_order_and_cut_tiles(ck, tq, tk, seqs, hq, hk, d, causal):
+    """Every other sequence claims all rows, at sizes whose tiles are cut: nothing outside the workspace and the tensors
+    is written."""
+    q, k, v, do = (t.cuda() for t in _attn_inputs([tq], [tk], hq, hk, d, tq + tk))
+    cu_q, cu_k = (_dev_cu([n if i % 2 else 0 for i in range(seqs + 1)]) for n in (tq, tk))
+    lib, guard = ck.lib(), 1 << 20
+    sizes = [f(seqs, tq, tk, hq, hk, d) for f in (lib.ck4_attention_workspace_bytes, lib.ck4_attention_backward_workspace_bytes)]
+    assert sizes[0] > 0
+    room = [torch.full((n + 2 * guard,), 0xA5, dtype=torch.uint8, device="cuda") for n in sizes]
+    ws = [r[guard:guard + n] for r, n in zip(room, sizes)]
+    bufs = [torch.full((x.shape[0] + 200, *x.shape[1:]), 3.0, dtype=BF16, device="cuda") for x in (q, q, k, k)]
+    views = [b[100:-100] for b in bufs]
+    out, lse = ck.attention(q, k, v, cu_q, cu_k, causal=causal, out=views[0], workspace=ws[0])
+    ck.attention_backward(do, q, k, v, out, lse, cu_q, cu_k, causal=causal, dq=views[1], dk=views[2], dv=views[3],
+                          workspace=ws[1])
+    for r, n in zip(room, sizes):
+        assert (r[:guard] == 0xA5).all() and (r[guard + n:] == 0xA5).all()
+    for b in bufs:
+        assert (b[:100] == 3).all() and (b[-100:] == 3).all()
+
+
 def test_attention_streams_and_graph(ck):
     """On a stream that is not the default one, and captured into a graph and replayed on new data."""
     t, hq, hk, d = 190, 4, 2, 64
