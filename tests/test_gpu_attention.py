@@ -107,6 +107,40 @@ def test_norm_rope_backward(ck, t, hq, hk, d, sections, interleaved, pos_f32):
         _near(dw, want_w, 2.0 ** -18 * size_w, f"d{name}_weight")
 
 
+# more steps than the launches have wavefronts (8192, and 4096 backward), in uneven shares that cross tokens
+NORMS_LONG = [
+    (1531, 24, 5, 128, (64,), False, False),       # 8 steps a token
+    (1531, 24, 5, 128, (8, 28, 28), True, False),
+    (1531, 24, 5, 128, (30, 31), False, True),     # half-split pairs that end inside a 16-byte chunk
+    (5003, 3, 2, 136, (68,), True, False),         # 2 heads a step: 3 steps a token, the last half full
+    (2311, 29, 12, 72, (32,), False, False),       # rotated in part, 4 heads a step, the last step a quarter full
+]
+
+
+@pytest.mark.parametrize("t,hq,hk,d,sections,interleaved,pos_f32", NORMS_LONG)
+def test_norm_rope_many_steps_a_wavefront(ck, t, hq, hk, d, sections, interleaved, pos_f32):
+    test_norm_rope(ck, t, hq, hk, d, sections, interleaved, pos_f32)
+    test_norm_rope_backward(ck, t, hq, hk, d, sections, interleaved, pos_f32)
+
+
+@pytest.mark.parametrize("t,hq,hk,d,sections,interleaved,pos_f32", NORMS_LONG)
+def test_norm_rope_many_steps_in_place(ck, t, hq, hk, d, sections, interleaved, pos_f32):
+    """Outputs that are the inputs, with the next heads loaded ahead of a store: the same bits; and twice the same."""
+    q, k, wq, wk, pos, freqs = (x.cuda() for x in _norm_inputs(t, hq, hk, d, sections, pos_f32, 500 + t + d))
+    g = _gen(t)
+    dyq, dyk = _rand(g, t, hq, d).cuda(), _rand(g, t, hk, d).cuda()
+    rest = (wq, wk, pos, freqs, sections, interleaved)
+    want, want_g = ck.qk_norm_rope(q, k, *rest), ck.qk_norm_rope_backward(dyq, dyk, q, k, *rest)
+    over = [x.clone() for x in (dyq, dyk)]
+    got_g = ck.qk_norm_rope_backward(*over, q, k, *rest, dq=over[0], dk=over[1])
+    assert got_g[0] is over[0] and all(torch.equal(a, b) for a, b in zip(_bits(*got_g), _bits(*want_g)))
+    over = [x.clone() for x in (q, k)]
+    got_g = ck.qk_norm_rope_backward(dyq, dyk, *over, *rest, dq=over[0], dk=over[1])
+    assert all(torch.equal(a, b) for a, b in zip(_bits(*got_g), _bits(*want_g)))
+    got = ck.qk_norm_rope(q, k, *rest, q_out=q, k_out=k)
+    assert got[0] is q and all(torch.equal(a, b) for a, b in zip(_bits(*got), _bits(*want)))
+
+
 def test_norm_rope_against_differences(ck):
     """The kernel's gradients along random directions against differences of the 64-bit forward pass."""
     t, h, d, sections = 6, 2, 64, (8, 12, 12)
