@@ -272,6 +272,27 @@ def test_attention_backward(ck, lens_q, lens_k, hq, hk, d, causal):
     assert all(torch.equal(a, b) for a, b in zip(_bits(*got), _bits(*again)))
 
 
+# more than 256 whole tiles of keys and of queries, none cut: a launch each for their gradients; numbers of heads of which
+# an XCD has several
+WHOLE = [
+    ([20] * 40, [20] * 40, 40, 8, 128, True),
+    ([300, 1, 0, 77] * 12, [310, 1, 5, 40] * 12, 16, 8, 64, True),
+    ([20] * 40, [33] * 40, 40, 8, 128, False),
+    ([5, 260] * 12, [260, 5] * 12, 24, 8, 72, False),
+    ([300, 20, 600] * 5, [300, 50, 600] * 5, 24, 24, 128, True),
+    ([300, 20, 600] * 5, [300, 50, 600] * 5, 24, 24, 40, True),
+]
+
+
+@pytest.mark.parametrize("lens_q,lens_k,hq,hk,d,causal", WHOLE)
+def test_attention_many_whole_tiles(ck, lens_q, lens_k, hq, hk, d, causal):
+    sizes = len(lens_q), sum(lens_q), sum(lens_k), hq, hk, d
+    assert ck.lib().ck4_attention_workspace_bytes(*sizes) == 0
+    assert ck.lib().ck4_attention_backward_workspace_bytes(*sizes) == 8 * sum(lens_q) * hq  # the rows' statistics alone
+    test_attention(ck, lens_q, lens_k, hq, hk, d, causal, 1.0)
+    test_attention_backward(ck, lens_q, lens_k, hq, hk, d, causal)
+
+
 def test_attention_against_differences(ck):
     """Forward and backward kernels together: gradients along random directions against differences in 64 bits."""
     lens_q, lens_k, hq, hk, d = [70, 9], [81, 5], 4, 2, 64
@@ -457,6 +478,12 @@ DECODES += [
     ([512, 300, 0], 512, 4, 2, 128), ([513, 1, 0, 257], 513, 4, 2, 128), ([2048, 2047, 33], 2048, 6, 2, 64),
     ([2049, 0, 31], 2049, 6, 2, 64), ([0, 3, 0, 0, 100, 0], 2100, 4, 2, 128), ([700, 1, 1300], 2200, 34, 1, 64),
     ([1900, 5], 2000, 20, 1, 128), ([50 + 29 * i for i in range(70)], 2064, 3, 1, 40), ([4096], 5000, 17, 1, 128),
+]
+
+# so many units that one group of threads joins each
+DECODES += [
+    ([2100, 0, 1, 700, 33] * 4, 2100, 40, 8, 128), ([100 + 97 * i for i in range(21)], 2065, 40, 8, 64),
+    ([2500 - 700 * (i % 4) for i in range(33)], 2500, 20, 4, 72),
 ]
 
 
