@@ -458,6 +458,29 @@ def test_attention_causal_nonfinite(ck, which, reach, at):
     assert out[at:].isnan().all()
 
 
+@pytest.mark.parametrize("n,hq,hk,d", [(700, 4, 2, 128), (1500, 4, 2, 64), (700, 24, 24, 72)])
+@pytest.mark.parametrize("at", [63, 64, 300])
+def test_attention_backward_causal_nonfinite(ck, n, hq, hk, d, at):
+    """NaN in one row of q, k, v or dout of a causal sequence: gradients that do not depend on it, and are further than
+    320 from it, are the same bits as without it."""
+    q, k, v, do = (x.cuda() for x in _attn_inputs([n], [n], hq, hk, d, at + n))
+    out, lse = ck.attention(q, k, v, causal=True)
+    want = ck.attention_backward(do, q, k, v, out, lse, causal=True)
+    for which in range(4):
+        x = [do, q, k, v]
+        x[which] = x[which].clone()
+        x[which][at] = math.inf if which % 2 else math.nan
+        got = ck.attention_backward(*x, *ck.attention(*x[1:], causal=True), causal=True)
+        if which < 2:  # a row: the other rows' dq, and the keys after it
+            free_q = torch.arange(n) != at
+            assert got[0][at].isnan().all()
+            after = slice(min(n, at + 321), None)
+            assert all(torch.equal(a[after], b[after]) for a, b in zip(_bits(*got[1:]), _bits(*want[1:])))
+        else:  # a key: the rows before it
+            free_q = torch.arange(n) < at - 320
+        assert torch.equal(_bits(got[0])[0][free_q], _bits(want[0])[0][free_q])
+
+
 # ------------------------------------------------------------ decoding
 
 # lengths, slots, hq, hk, d
