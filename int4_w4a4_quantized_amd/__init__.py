@@ -1003,6 +1003,11 @@ def _workspace(workspace, need: int, like):
     return like.new_empty(need, dtype=torch.uint8) if workspace is None and need else workspace
 
 
+def _extent(workspace):
+    """(pointer, bytes) of a workspace; none for sizes that need none, or that the library refuses."""
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+
+
 def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, q_weight, k_weight,
                           positions: torch.Tensor, freqs: torch.Tensor, sections=None, interleaved: bool = True,
                           eps: float = 1e-6, dq=None, dk=None, workspace=None):
@@ -1028,8 +1033,8 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     _check("ck4_qk_norm_rope_backward",
            L.ck4_qk_norm_rope_backward(*dqo, *dko, *qa, *ka, t, hq, hk, d, qw, kw, pos, pos_f32, axes, secs, fr,
-                                       bool(interleaved), eps, *dqa, *dka, _opt(dqw), _opt(dkw), workspace.data_ptr(),
-                                       workspace.numel(), stream))
+                                       bool(interleaved), eps, *dqa, *dka, _opt(dqw), _opt(dkw), *_extent(workspace),
+                                       stream))
     return dq, dk, dqw, dkw
 
 
@@ -1086,10 +1091,10 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q=None, cu_k
     if lse is None:
         lse = q.new_empty((hq, tq), dtype=_F32)
     workspace = _workspace(workspace, L.ck4_attention_workspace_bytes(seqs, tq, tk, hq, hk, d), q)
-    wa, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _check("ck4_attention",
            L.ck4_attention(*qa, *ka, *va, _opt(cu_q), _opt(cu_k), seqs, tq, tk, hq, hk, d, bool(causal),
-                           d ** -0.5 if scale is None else scale, *oa, lse.data_ptr(), wa, wn, stream))
+                           d ** -0.5 if scale is None else scale, *oa, lse.data_ptr(), *_extent(workspace),
+                           stream))
     return out, lse
 
 
@@ -1120,8 +1125,9 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     tk, hk, _ = k.shape
     workspace = _workspace(workspace, L.ck4_attention_backward_workspace_bytes(seqs, tq, tk, hq, hk, d), q)
     _check("ck4_attention_backward",
-           L.ck4_attention_backward(*ga, *qa, *ka, *va, *oa, la, _opt(cu_q), _opt(cu_k), seqs, tq, tk, hq, hk, d, bool(causal), d ** -0.5 if scale is None else scale, *dqa, *dka,
-                                    *dva, workspace.data_ptr(), workspace.numel(), stream))
+           L.ck4_attention_backward(*ga, *qa, *ka, *va, *oa, la, _opt(cu_q), _opt(cu_k), seqs, tq, tk, hq, hk, d,
+                                    bool(causal), d ** -0.5 if scale is None else scale, *dqa, *dka, *dva,
+                                    *_extent(workspace), stream))
     return dq, dk, dv
 
 
@@ -1158,10 +1164,9 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         lse = q.new_empty((hq, b), dtype=_F32)
     L = lib()
     workspace = _workspace(workspace, L.ck4_attention_decode_workspace_bytes(b, slots, hq, hk, d), q)
-    wa, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     ks, vs = k_cache.stride(), v_cache.stride()
     _check("ck4_attention_decode",
            L.ck4_attention_decode(*qa, k_cache.data_ptr(), ks[0], ks[1], ks[2], v_cache.data_ptr(), vs[0], vs[1], vs[2], na,
-                                  b, slots, hq, hk, d, d ** -0.5 if scale is None else scale, *oa, lse.data_ptr(), wa, wn,
-                                  stream))
+                                  b, slots, hq, hk, d, d ** -0.5 if scale is None else scale, *oa, lse.data_ptr(),
+                                  *_extent(workspace), stream))
     return out, lse

@@ -128,7 +128,7 @@ ck4_status ck4_qk_norm_rope_backward(const uint16_t *dq_out, int64_t dqo_st, int
                                      size_t ws_bytes, void *stream) {
     const char *fn = "ck4_qk_norm_rope_backward";
     ck4::NormRope a{};
-    if (!dq_out || !dk_out || !dq || !dk || !workspace) return api_fail(CK4_ERR_INVALID, "%s: null pointer", fn);
+    if (!dq_out || !dk_out || !dq || !dk) return api_fail(CK4_ERR_INVALID, "%s: null pointer", fn);
     if (ck4_status s = check_norm_rope(fn, tokens, hq, hk, d, q, k, q_weight, k_weight, positions, axes, sections, freqs,
                                        eps, &a))
         return s;
@@ -141,8 +141,8 @@ ck4_status ck4_qk_norm_rope_backward(const uint16_t *dq_out, int64_t dqo_st, int
     if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4) || !aligned(workspace, 4))
         return api_fail(CK4_ERR_INVALID, "%s: dq_weight, dk_weight or workspace not 4-byte aligned", fn);
     const size_t need = ck4_qk_norm_rope_workspace_bytes(tokens, d);
-    if (ws_bytes < need)
-        return api_fail(CK4_ERR_INVALID, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
+    if (!workspace || ws_bytes < need)
+        return api_fail(CK4_ERR_INVALID, "%s: workspace %zu bytes < %zu needed", fn, workspace ? ws_bytes : 0, need);
     if (ck4_status s = ck4::api_check_device(fn, nullptr)) return s;
     a.x[0] = {q, q_st, q_sh};
     a.x[1] = {k, k_st, k_sh};
@@ -245,7 +245,7 @@ ck4_status ck4_attention_backward(const uint16_t *dout, int64_t do_st, int64_t d
                                   int64_t dv_sh, void *workspace, size_t ws_bytes, void *stream) {
     const char *fn = "ck4_attention_backward";
     ck4::Attn a{};
-    if (!dout || !out || !lse || !dq || !dk || !dv || !workspace)
+    if (!dout || !out || !lse || !dq || !dk || !dv)
         return api_fail(CK4_ERR_INVALID, "%s: null pointer", fn);
     if (ck4_status s = check_attention(fn, q, &q_st, &q_sh, k, &k_st, &k_sh, v, &v_st, &v_sh, cu_q, cu_k, seqs, tq, tk, hq,
                                        hk, d, causal, scale, &a))
@@ -258,8 +258,8 @@ ck4_status ck4_attention_backward(const uint16_t *dout, int64_t do_st, int64_t d
     if (!aligned(lse, 4) || !aligned(workspace, 16))
         return api_fail(CK4_ERR_INVALID, "%s: lse or workspace misaligned", fn);
     const size_t need = ck4_attention_backward_workspace_bytes(seqs, tq, tk, hq, hk, d);
-    if (ws_bytes < need)
-        return api_fail(CK4_ERR_INVALID, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
+    if (!workspace || ws_bytes < need)
+        return api_fail(CK4_ERR_INVALID, "%s: workspace %zu bytes < %zu needed", fn, workspace ? ws_bytes : 0, need);
     if (ck4_status s = ck4::api_check_device(fn, nullptr)) return s;
     return ck4::api_launched(
         fn, ck4::launch_attention_backward(a, {out, o_st, o_sh}, {dout, do_st, do_sh}, lse, static_cast<float *>(workspace),

@@ -170,3 +170,27 @@ def test_workspace_sizes():
     assert L.ck4_attention_decode_workspace_bytes(2, 5000, 5, 2, 64) == 0  # heads do not divide
     assert L.ck4_attention_decode_workspace_bytes(2, 100, 4, 2, 64) == 0  # short: units are not cut
     assert L.ck4_attention_decode_workspace_bytes(2, 5000, 4, 2, 64) > 0
+
+
+@pytest.mark.parametrize("t,d", [(4, 264), (4, 60), (0, 64)])
+def test_norm_gradients_refuse_sizes_without_a_workspace(monkeypatch, t, d):
+    """Sizes that no workspace is given for end in the library's error, as in the forward call (host tensors: nothing is
+    launched)."""
+    monkeypatch.setattr(ck, "_gpu_stream", lambda *a: None)
+    q, k, pos, freqs = _h(t, 3, d), _h(t, 2, d), torch.zeros(t, 1, dtype=I32), torch.ones(4)
+    with pytest.raises(ck.Ck4Error) as fwd:
+        ck.qk_norm_rope(q, k, None, None, pos, freqs)
+    with pytest.raises(ck.Ck4Error) as bwd:
+        ck.qk_norm_rope_backward(q, k, q, k, None, None, pos, freqs)
+    assert bwd.value.status == fwd.value.status
+
+
+@pytest.mark.parametrize("tq,tk,hk,d", [(6, 8, 2, 136), (6, 8, 2, 60), (6, 8, 3, 64), (0, 8, 2, 64), (6, 0, 2, 64)])
+def test_attention_gradients_refuse_sizes_without_a_workspace(monkeypatch, tq, tk, hk, d):
+    monkeypatch.setattr(ck, "_gpu_stream", lambda *a: None)
+    q, k, lse = _h(tq, 4, d), _h(tk, hk, d), torch.zeros(4, tq)
+    with pytest.raises(ck.Ck4Error) as fwd:
+        ck.attention(q, k, k)
+    with pytest.raises(ck.Ck4Error) as bwd:
+        ck.attention_backward(q, q, k, k, q, lse)
+    assert bwd.value.status == fwd.value.status
