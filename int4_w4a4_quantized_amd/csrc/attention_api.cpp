@@ -114,7 +114,7 @@ ck4_status ck4_qk_norm_rope(const uint16_t *q, int64_t q_st, int64_t q_sh, const
 }
 
 size_t ck4_qk_norm_rope_workspace_bytes(int64_t tokens, int d) {
-    if (tokens <= 0 || tokens > kMaxTokens || d <= 0 || d > 256) return 0;
+    if (tokens <= 0 || tokens > kMaxTokens || d <= 0 || d % 8 != 0 || d > 256) return 0;
     return (size_t)ck4::qk_norm_rope_blocks(tokens) * 2 * d * sizeof(float);
 }
 
@@ -159,6 +159,12 @@ ck4_status ck4_qk_norm_rope_backward(const uint16_t *dq_out, int64_t dqo_st, int
 
 namespace {
 
+// The kernels count tiles of 256 rows per head, and steps of 64, in 32 bits: so many of 64, and a part tile of queries
+// and one of keys per sequence, are more than one launch takes.
+bool too_many_tiles(int64_t seqs, int64_t tq, int64_t tk, int hq) {
+    return (tq / 64 + tk / 64 + 2 * seqs + 2) * hq > INT32_MAX / 2;
+}
+
 // Shapes, strides and options that the attention calls share.
 ck4_status check_attention(const char *fn, const uint16_t *q, int64_t *q_st, int64_t *q_sh, const uint16_t *k,
                            int64_t *k_st, int64_t *k_sh, const uint16_t *v, int64_t *v_st, int64_t *v_sh,
@@ -176,8 +182,7 @@ ck4_status check_attention(const char *fn, const uint16_t *q, int64_t *q_st, int
         return api_fail(CK4_ERR_UNSUPPORTED, "%s: d=%d (need a multiple of 8 up to 128)", fn, d);
     if (tq > kMaxTokens || tk > kMaxTokens || hq > kMaxHeads || seqs > (1 << 20))
         return api_fail(CK4_ERR_UNSUPPORTED, "%s: too many tokens, heads or sequences", fn);
-    // a workgroup per head and tile of at least 128 rows, plus a part tile per sequence
-    if ((tq / 64 + tk / 64 + 2 * seqs + 2) * hq > INT32_MAX / 2)
+    if (too_many_tiles(seqs, tq, tk, hq))
         return api_fail(CK4_ERR_UNSUPPORTED, "%s: too many tiles for one launch", fn);
     if (ck4_status s = check_heads(fn, "q", q, tq, hq, d, q_st, q_sh, false)) return s;
     if (ck4_status s = check_heads(fn, "k", k, tk, hk, d, k_st, k_sh, false)) return s;
@@ -197,7 +202,8 @@ ck4_status check_attention(const char *fn, const uint16_t *q, int64_t *q_st, int
 // Whether the sizes are ones that a workspace size is given for (the calls check them again).
 bool attention_sizes(int64_t seqs, int64_t tq, int64_t tk, int hq, int hk, int d) {
     return seqs > 0 && seqs <= (1 << 20) && tq > 0 && tq <= kMaxTokens && tk > 0 && tk <= kMaxTokens && hq > 0 &&
-           hq <= kMaxHeads && hk > 0 && hq % hk == 0 && d > 0 && d <= 128;
+           hq <= kMaxHeads && hk > 0 && hq % hk == 0 && d > 0 && d % 8 == 0 && d <= 128 &&
+           !too_many_tiles(seqs, tq, tk, hq);
 }
 
 }  // namespace
@@ -280,12 +286,19 @@ ck4_status check_batch_stride(const char *fn, const char *name, int64_t batch, i
     return CK4_OK;
 }
 
+// The kernels count query heads, and tiles of 32 slots per sequence and key head (or 16 query heads), in 32 bits.
+bool decode_too_large(int64_t batch, int64_t slots, int hq, int hk) {
+    return batch > (1 << 20) || slots > kMaxTokens || hq > kMaxHeads || batch * hq > INT32_MAX ||
+           batch * (hk + hq / 16 + 1) * (slots / 32 + 1) > INT32_MAX / 2;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t ck4_attention_decode_workspace_bytes(int64_t batch, int64_t slots, int hq, int hk, int d) {
-    if (batch <= 0 || batch > (1 << 20) || slots <= 0 || slots > kMaxTokens || hq <= 0 || hk <= 0 || hq > kMaxHeads || hq % hk != 0 || d <= 0 || d > 128)
+    if (batch <= 0 || slots <= 0 || hq <= 0 || hk <= 0 || hq % hk != 0 || d <= 0 || d % 8 != 0 || d > 128 ||
+        decode_too_large(batch, slots, hq, hk))
         return 0;
     return (size_t)ck4::attention_decode_floats(batch, slots, hq, hk, d) * sizeof(float);
 }
@@ -303,11 +316,8 @@ ck4_status ck4_attention_decode(const uint16_t *q, int64_t q_st, int64_t q_sh, c
     if (hq % hk != 0) return api_fail(CK4_ERR_INVALID, "%s: hq=%d is not a multiple of hk=%d", fn, hq, hk);
     if (d % 8 != 0 || d > 128)
         return api_fail(CK4_ERR_UNSUPPORTED, "%s: d=%d (need a multiple of 8 up to 128)", fn, d);
-    if (batch > (1 << 20) || slots > kMaxTokens || hq > kMaxHeads || batch * hq > INT32_MAX)
+    if (decode_too_large(batch, slots, hq, hk))
         return api_fail(CK4_ERR_UNSUPPORTED, "%s: batch, slots or heads too large", fn);
-    // the kernels count tiles of 32 slots, per sequence and key head (or 16 query heads), in 32 bits
-    if (batch * (hk + hq / 16 + 1) * (slots / 32 + 1) > INT32_MAX / 2)
-        return api_fail(CK4_ERR_UNSUPPORTED, "%s: the cache is too large", fn);
     if (ck4_status s = check_heads(fn, "q", q, batch, hq, d, &q_st, &q_sh, false)) return s;
     if (ck4_status s = check_heads(fn, "k", k, slots, hk, d, &k_st, &k_sh, false)) return s;
     if (ck4_status s = check_heads(fn, "v", v, slots, hk, d, &v_st, &v_sh, false)) return s;

@@ -194,3 +194,27 @@ def test_attention_gradients_refuse_sizes_without_a_workspace(monkeypatch, tq, t
     with pytest.raises(ck.Ck4Error) as bwd:
         ck.attention_backward(q, q, k, k, q, lse)
     assert bwd.value.status == fwd.value.status
+
+
+def test_no_workspace_size_for_refused_sizes():
+    """The sizes are 0 where the calls refuse them: heads that are no multiple of 8, and more tiles than a launch takes."""
+    L = ck.lib()
+    big = 1 << 60
+    norm = dict(dqo=P, x=192, y=64, dko=P, z=128, w=64, q=P, q_st=192, q_sh=64, k=P, k_st=128, k_sh=64, tokens=4, hq=3,
+                hk=2, d=60, qw=None, kw=None, pos=P, f32=0, axes=1, secs=SECS, freqs=P, inter=1, eps=1e-6, dq=P, dq_st=192,
+                dq_sh=64, dk=P, dk_st=128, dk_sh=64, dqw=P, dkw=P, ws=P, ws_bytes=big, stream=None)
+    assert L.ck4_qk_norm_rope_backward(*norm.values()) == UNS
+    assert L.ck4_qk_norm_rope_workspace_bytes(4, 60) == 0
+    for seqs, tq, tk, hq, hk, d in [(3, 2000, 2000, 4, 2, 60), (1, 1 << 30, 8, 4096, 4096, 8), (1 << 20, 8, 8, 4096, 8, 64),
+                                    (1, 8, 1 << 30, 4096, 4096, 8)]:
+        q, k = (max(st, 8) for st in (hq * d, hk * d))
+        good = {**ATTN, "seqs": seqs, "tq": tq, "tk": tk, "hq": hq, "hk": hk, "d": d, "q_st": q, "k_st": k, "v_st": k,
+                "o_st": q, "q_sh": d, "k_sh": d, "v_sh": d, "o_sh": d, "ws": P, "ws_bytes": big}
+        assert L.ck4_attention(*good.values()) == UNS
+        assert L.ck4_attention_workspace_bytes(seqs, tq, tk, hq, hk, d) == 0
+        assert L.ck4_attention_backward_workspace_bytes(seqs, tq, tk, hq, hk, d) == 0
+    for batch, slots, hq, hk, d in [(2, 5000, 4, 2, 60), (1 << 20, 5000, 4096, 8, 64), (1 << 20, 1 << 30, 1, 1, 64)]:
+        good = {**DEC, "batch": batch, "slots": slots, "hq": hq, "hk": hk, "d": d, "q_st": hq * d, "q_sh": d,
+                "k_st": hk * d, "k_sh": d, "v_st": hk * d, "v_sh": d, "o_st": hq * d, "o_sh": d, "ws_bytes": big}
+        assert L.ck4_attention_decode(*good.values()) == UNS
+        assert L.ck4_attention_decode_workspace_bytes(batch, slots, hq, hk, d) == 0
