@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -932,6 +933,9 @@ def _gpu_stream(names: str, *tensors):
 
 @functools.lru_cache(maxsize=64)
 def _host_ints(values: tuple):
+    """A host array of ints, and their sum."""
+    if any(v != ctypes.c_int(v).value for v in values):
+        raise ValueError(f"sections must be 32-bit whole numbers, got {values}")
     return (ctypes.c_int * len(values))(*values), sum(values)
 
 
@@ -944,7 +948,10 @@ def _rope_args(tokens: int, d: int, q_weight, k_weight, positions, freqs, sectio
     if not isinstance(freqs, torch.Tensor) or freqs.dtype is not _F32 or freqs.dim() != 1 or not freqs.is_contiguous():
         _dense(freqs, _F32, "freqs", 1)
     pairs = freqs.shape[0]
-    secs, total = _host_ints((pairs,) if sections is None else tuple(sections))
+    try:
+        secs, total = _host_ints((pairs,) if sections is None else tuple(map(operator.index, sections)))
+    except TypeError:
+        raise ValueError(f"sections must be whole numbers, one an axis, got {sections!r}") from None
     axes = len(secs)
     if positions.shape != (tokens, axes) and not (axes == 1 and positions.shape == (tokens,)):
         raise ValueError(f"positions must have shape {(tokens, axes)}, got {tuple(positions.shape)}")

@@ -218,3 +218,14 @@ def test_no_workspace_size_for_refused_sizes():
                 "k_st": hk * d, "k_sh": d, "v_st": hk * d, "v_sh": d, "o_st": hq * d, "o_sh": d, "ws_bytes": big}
         assert L.ck4_attention_decode(*good.values()) == UNS
         assert L.ck4_attention_decode_workspace_bytes(batch, slots, hq, hk, d) == 0
+
+
+@pytest.mark.parametrize("sections", [(64.0,), (20.5, 43.5), ("64",), (None,), 64, (1 << 32, 64 - (1 << 32))])
+def test_sections_are_whole_numbers(monkeypatch, sections):
+    """Whatever sections an earlier call had: a float that equals a whole number is refused too."""
+    monkeypatch.setattr(ck, "_gpu_stream", lambda *a: None)
+    monkeypatch.setattr(ck, "lib", lambda: pytest.fail("the library was called"))
+    ck._host_ints((64,))
+    q, pos = _h(4, 1, 128), torch.zeros(4, 2 if isinstance(sections, tuple) and len(sections) == 2 else 1, dtype=I32)
+    with pytest.raises(ValueError, match="sections"):
+        ck.qk_norm_rope(q, q, None, None, pos, torch.ones(64), sections)
