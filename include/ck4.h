@@ -561,7 +561,7 @@ ck4_status ck4_linear_w4a4_fp6c_lora(const uint8_t *x_q6c, const float *x_scales
  *   sections   host int [axes]: axis a turns the next sections[a] pairs (one
  *              axis for texts; time, height and width for images and video).
  *              pairs = their sum, at most d / 2.
- *   freqs      fp32 [pairs].
+ *   freqs      fp32 [pairs]; may be NULL if no pair is turned (the norm alone).
  *   interleaved  pair j is (2j, 2j + 1), else (j, j + pairs); elements from
  *              2 * pairs on are normalised only.
  *   q_out, k_out  may be q and k (same strides).

@@ -49,7 +49,7 @@ ck4_status check_scale(const char *fn, float scale) {
 ck4_status check_norm_rope(const char *fn, int64_t tokens, int hq, int hk, int d, const void *q, const void *k,
                            const float *q_weight, const float *k_weight, const void *positions, int axes,
                            const int *sections, const float *freqs, float eps, ck4::NormRope *a) {
-    if (!q || !k || !positions || !sections || !freqs) return api_fail(CK4_ERR_INVALID, "%s: null pointer", fn);
+    if (!q || !k || !positions || !sections) return api_fail(CK4_ERR_INVALID, "%s: null pointer", fn);
     if (tokens <= 0 || hq <= 0 || hk <= 0 || d <= 0)
         return api_fail(CK4_ERR_INVALID, "%s: tokens, hq, hk and d must be positive", fn);
     if (!(eps >= 0.0f) || !std::isfinite(eps)) return api_fail(CK4_ERR_INVALID, "%s: eps=%g", fn, (double)eps);
@@ -69,6 +69,7 @@ ck4_status check_norm_rope(const char *fn, int64_t tokens, int hq, int hk, int d
         }
         a->rope.end[i] = pairs;
     }
+    if (pairs > 0 && !freqs) return api_fail(CK4_ERR_INVALID, "%s: null pointer", fn);
     if (!aligned(positions, 4) || !aligned(freqs, 4) || !aligned(q_weight, 4) || !aligned(k_weight, 4))
         return api_fail(CK4_ERR_INVALID, "%s: positions, freqs or a weight not 4-byte aligned", fn);
     a->tokens = tokens;

@@ -83,6 +83,11 @@ int main() {
     const int secs[4] = {8, 8, 8, 8};
     expect("norm", norm(256, 64, 5, 4, 64, secs), true);
     expect("norm, one token and head", norm(INT64_MIN / 8 * 8, INT64_MIN / 8 * 8, 1, 1, 64, secs), true);
+    const int none[4] = {0, 0, 0, 0};  // no pair is turned: no frequencies
+    expect("norm without rotation", ck4_qk_norm_rope(p, 256, 64, p, 256, 64, 5, 4, 4, 64, f, f, n, 0, 4, none, nullptr, 1,
+                                                     1e-6f, p, 256, 64, p, 256, 64, nullptr), true);
+    expect("norm without frequencies", ck4_qk_norm_rope(p, 256, 64, p, 256, 64, 5, 4, 4, 64, f, f, n, 0, 4, secs, nullptr, 1,
+                                                        1e-6f, p, 256, 64, p, 256, 64, nullptr), false);
     expect("norm_bwd", norm_bwd(256, 64, 5, 4, 64, secs), true);
     expect("attn", attn(256, 64, 5, 4, 64, 3), true);
     expect("attn, heads first", attn(64, 320, 5, 4, 64, 3), true);

@@ -164,6 +164,15 @@ def test_norm_rope_against_differences(ck):
     assert abs((dwq * uw).sum().item() - diff) <= 1e-4 * (dwq * uw).abs().sum().item()
 
 
+@pytest.mark.parametrize("sections", [(0,), (0, 0, 0)])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_norm_without_rotation(ck, sections, interleaved):
+    """No pair is turned: the norm and its gradients alone."""
+    shape = 37, 5, 2, 72, sections, interleaved, False
+    test_norm_rope(ck, *shape)
+    test_norm_rope_backward(ck, *shape)
+
+
 def test_norm_rope_views_and_in_place(ck):
     """A fused projection's rows as inputs, a joint buffer and the inputs themselves as outputs: the same bits."""
     t, hq, hk, d = 70, 6, 2, 96
