@@ -10,9 +10,9 @@ namespace ck4 {
 
 // Sets ck4_last_error() and returns s.
 ck4_status api_fail(ck4_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-// CK4_OK if the current device is a gfx950, else CK4_ERR_DEVICE. Its number of
-// compute units goes to *cus if cus is not null.
-ck4_status api_check_device(const char *fn, int *cus);
+// CK4_OK if the current device is a gfx950, else CK4_ERR_DEVICE. Its number
+// goes to *dev if dev is not null.
+ck4_status api_check_device(const char *fn, int *dev);
 // The status of a launch: CK4_OK clears ck4_last_error().
 ck4_status api_launched(const char *fn, hipError_t e);
 

@@ -67,7 +67,6 @@ constexpr int kMaxDevices = 64;
 std::once_flag g_dev_once[kMaxDevices];
 int g_dev_ok[kMaxDevices];
 int64_t g_l2_bytes[kMaxDevices];
-int g_cus[kMaxDevices];
 
 // The kernels are built for gfx950 only; refuse any other device.
 ck4_status check_device(const char *fn, int *dev_out = nullptr) {
@@ -82,7 +81,6 @@ ck4_status check_device(const char *fn, int *dev_out = nullptr) {
         }
         g_dev_ok[dev] = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 0;
         g_l2_bytes[dev] = prop.l2CacheSize;
-        g_cus[dev] = prop.multiProcessorCount;
     });
     if (!g_dev_ok[dev]) return fail(CK4_ERR_DEVICE, "%s: current device is not gfx950", fn);
     if (dev_out) *dev_out = dev;
@@ -142,12 +140,7 @@ ck4_status api_fail(ck4_status s, const char *fmt, ...) {
     return s;
 }
 
-ck4_status api_check_device(const char *fn, int *cus) {
-    int dev = 0;
-    if (ck4_status s = check_device(fn, &dev)) return s;
-    if (cus) *cus = g_cus[dev];
-    return CK4_OK;
-}
+ck4_status api_check_device(const char *fn, int *dev) { return check_device(fn, dev); }
 
 ck4_status api_launched(const char *fn, hipError_t e) { return launched(fn, e); }
 
