@@ -60,7 +60,8 @@ class Block:
         return self.output(out)
 
     def gradients(self, x, cu, positions, dout):
-        """Gradients of the attention part (from the heads that the projections gave to the heads it returns)."""
+        """Gradients of the attention part (from the heads that the projections gave to the heads it returns): they end there,
+        as the quantised projections have none."""
         q, k, v = self.project(x)
         qn, kn = self.norm(q, k, positions)
         out, lse = ck.attention(qn, kn, v, cu, cu, causal=True)

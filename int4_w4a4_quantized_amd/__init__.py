@@ -883,6 +883,11 @@ def w4a4_lora_linear_fp6c(x: torch.Tensor, w_q6c: torch.Tensor, w_scales: torch.
 # Heads are bf16 [tokens, heads, d] tensors with unit stride in d; tokens and
 # heads may be strided (views of a fused projection's rows, slices of a joint
 # buffer), in multiples of 8 elements from a 16-byte aligned start.
+#
+# As all calls of this library, these record no autograd history: a result has
+# none, whether or not an argument requires a gradient. Gradients are what the
+# _backward calls return, from these operators' outputs to their inputs; the
+# quantised projections have no gradients.
 
 # These calls run between small kernels at decode sizes, so their checks stay
 # at a few attribute reads a tensor.
@@ -988,7 +993,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, positions
     how many pairs follow each axis, in order (default: all follow one).
     interleaved: pairs (2j, 2j + 1), else (j, j + pairs); elements past the
     pairs are normalised only. Returns (q_out, k_out), bf16; q_out and k_out
-    may be given, also as q and k themselves.
+    may be given, also as q and k themselves. No autograd history is recorded:
+    gradients are qk_norm_rope_backward's.
     """
     t, hq, hk, d, qa, ka = _qk_shapes(q, k)
     qw, kw, pos, pos_f32, axes, secs, fr = _rope_args(t, d, q_weight, k_weight, positions, freqs, sections)
@@ -1078,7 +1084,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q=None, cu_k
     sequence with nq queries and nk keys sees the keys j <= i + nk - nq.
     scale: default 1 / sqrt(d). Returns (out bf16 [tq, hq, d], lse fp32
     [hq, tq]): lse is the log-sum-exp of a row's scaled scores, which the
-    backward pass takes. A row that sees nothing has out 0 and lse -inf.
+    backward pass takes. A row that sees nothing has out 0 and lse -inf. No
+    autograd history is recorded: gradients are attention_backward's.
     workspace: uint8, ck4_attention_workspace_bytes (default: allocated here
     where that is not 0).
     """
@@ -1147,8 +1154,9 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     [batch] on the GPU: the filled slots of each sequence, from slot 0 on
     (what the other slots hold, NaN included, does not matter). Returns (out
     bf16 [batch, hq, d], lse fp32 [hq, batch]); a sequence of length 0 has out
-    0 and lse -inf. workspace: uint8, ck4_attention_decode_workspace_bytes
-    (default: allocated here where that is not 0).
+    0 and lse -inf. No autograd history is recorded, and there are no gradients.
+    workspace: uint8, ck4_attention_decode_workspace_bytes (default: allocated
+    here where that is not 0).
     """
     qa = _heads(q, "q")
     b, hq, d = q.shape

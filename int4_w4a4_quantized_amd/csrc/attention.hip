@@ -126,6 +126,8 @@ __device__ __forceinline__ void attn_fwd_part(const Attn &a, const HeadsOut &out
                 for (int j = 0; j < 16; ++j) o[b][j] *= f;
         }
     };
+    // P goes to bf16, as V is: the matrix unit multiplies operands of one type, and fp32 at 1/16 of the rate. The sum l
+    // takes the unrounded values. Against 64 bits the output is off by 0.0023 of itself, by 0.0017 if it alone were rounded.
     const auto weights = [&](const f32x16 x[2], bf16x8 w[4]) {
         const float mc = m * c;
 #pragma unroll

@@ -272,7 +272,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_decode_kernel(Decode a, fl
                 for (int j = 0; j < 4; ++j) {
                     const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(p[n][j], c, -mc));
                     l += e;
-                    w[4 * n + j] = (__bf16)e;
+                    w[4 * n + j] = (__bf16)e;  // for the product with V, as in attention.hip
                 }
             if (more)
                 wait_copies<kLoads>();  // V is there, the next K may be on its way
