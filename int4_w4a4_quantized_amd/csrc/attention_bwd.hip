@@ -13,10 +13,10 @@
 // operands are bf16 as well); all sums are fp32.
 //
 // Bound: the matrix unit's turns. At 4608 tokens, 24 heads of 128 (913 GFLOP in
-// 7 products): 14 us for D, 395 us for the query tiles (990 TFLOP/s) and 605 us
-// for the key tiles (860 TFLOP/s) at about 2 GHz, the matrix unit busy in 57 %
-// and 47 % of the cycles that a compute unit works; 432 tiles on 256 units
-// leave 16 % of them idle.
+// 7 products), calls apart, at about 2 GHz: 14 us for D, 634 us for the key tiles
+// (820 TFLOP/s) and 389 us for the query tiles (1.01 PFLOP/s); 917 us for all
+// three in a row of calls. Compute units work in 80 % of the time (432 tiles on
+// 256 of them), the matrix unit in 48 % and 61 % of that.
 #include <hip/hip_runtime.h>
 
 #include "attn_tile.h"

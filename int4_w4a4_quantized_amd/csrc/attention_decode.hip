@@ -2,8 +2,9 @@
 //
 // HBM-bound: every filled slot of the cache is read once, 4 d bytes per key
 // head, for 4 d operations per query head. 64 sequences of 300 to 16001 slots,
-// 8 key heads of 128: 246 us, 5.4 TB/s; one sequence of 5003 slots: 10.9 us, and
-// 3.8 us to join the parts, bound by launches and one copy's latency.
+// 8 key heads of 128: 246 us, 5.4 TB/s; one sequence of 5003 slots: 11.1 us, and
+// 4.0 us to join the parts, bound by launches and two rounds of copies' latency
+// (4.9 tiles a piece on 4 wavefronts).
 //
 // The slots of all (sequence, key head) units form one line of 32-slot tiles, cut into equal pieces, one per
 // workgroup, whatever the lengths: a piece may end inside a unit, and a unit
@@ -22,11 +23,11 @@ constexpr int kSlots = 32;    // slots of a tile: one wavefront's
 constexpr int kCols = 16;     // query heads of a unit
 constexpr int kWaves = 4;     // of a workgroup on the line
 constexpr int kGroups = 512;  // workgroups on the line at most
-// Caches of up to kShort slots are dealt whole units: no partial results and no second kernel, whose launch takes as long as
-// the products. Up to kShorter with 4 wavefronts a unit, two workgroups a compute unit (64 sequences of 20 to 512 slots, 40/8
-// heads: 15.7 us, with 8 wavefronts 16.5), else with 8, which have 8 tiles each at most (1024 slots: 16.7 us on the line, 11.8
-// with 8 and 11.9 with 4 wavefronts; 2048 slots: 16.6, 15.2, 20.3; 16 sequences of 100 to 2000: 23.3, 14.7, 17.5; 4096 slots:
-// 16.0 on the line, 27.2 with 8 wavefronts).
+// Caches of up to kShort slots, by their size, as the lengths are on the device, are dealt whole units: no partial results
+// and no second kernel, whose launch takes as long as the products. Up to kShorter with 4 wavefronts a unit, two workgroups a
+// compute unit (64 sequences of 20 to 512 slots, 40/8 heads: 15.7 us, with 8 wavefronts 16.5), else with 8, which have 8 tiles
+// each at most (full caches of 1024 slots: 16.7 us on the line, 11.8 with 8 and 11.9 with 4 wavefronts; 2048 slots: 16.6,
+// 15.2, 20.3; 16 sequences of 100 to 2000: 23.3, 14.7, 17.5; 4096 slots: 16.0 on the line, 27.2 with 8 wavefronts).
 constexpr int kShorter = 512, kShort = 2048;
 constexpr float kSlackD = 8.0f;   // see attention.hip
 constexpr float kNoMaxD = -1e30f;

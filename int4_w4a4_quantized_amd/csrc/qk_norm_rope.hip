@@ -10,7 +10,7 @@
 //
 // Both directions are one pass over the heads and HBM-bound: 4 bytes an
 // element forward, 6 backward. 4608 tokens of 24 + 24 heads of 128: forward
-// 21.5 us (5.3 TB/s), backward 34.0 us (5.0 TB/s) and 4.1 us for the join of
+// 21.7 us (5.2 TB/s), backward 35.1 us (4.8 TB/s) and 4.1 us for the join of
 // the weight gradients. A head lives in GL lanes of one wavefront, 8
 // elements (16 bytes) a lane, so its sums are a few cross-lane adds and no
 // data is staged. All sums are fp32, and outputs are rounded to bf16 once.
